@@ -773,7 +773,9 @@ __global__ void __launch_bounds__(kThreads, 1)
               if (masked) vis[q] &= draft_bits(a, sq.q0 + i, k0 - dbase);
             }
           }
-          const float ft = f_row * exp2i(ti.k_exp - kNorm);
+          // never 0, which would turn hidden keys' -inf into NaN: zero queries over small keys reach 2^-215
+          // (scores are below 2^37 in these units, so a larger ft leaves them at 0 all the same)
+          const float ft = fmaxf(f_row * exp2i(ti.k_exp - kNorm), 0x1p-126f);
           if (!full) {  // hidden keys' scores become -inf, in TMEM
 #pragma unroll 1
             for (int q = 0; q < kKeys / 16; ++q) {
@@ -800,7 +802,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int o = 0; o < 2; ++o) {
               tc::tmem_wait_ld(x);
               float mx = max32(x);
-              if (mx != -CUDART_INF_F) mx *= ft;  // (ft may have underflowed)
+              mx *= ft;  // (-inf stays: ft > 0)
               const bool grow = mx > m + kLag;
               if (__any_sync(0xFFFFFFFFu, grow)) {
                 const float f = grow && m != -CUDART_INF_F ? ex2(m - mx) : 1.0f;

@@ -1,0 +1,58 @@
+"""GPU tests of the attention operators at values and masks where one key, row or element must not reach another:
+zero and tiny scores, cache contents that no row sees, extreme windows and queries, copied elements."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from test_gpu_attention import DT, STEP, build_cache, check, gen, reference, w4  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def i32(*v):
+    return torch.tensor(v, dtype=torch.int32, device="cuda")
+
+
+def packed(bits):
+    """Truth values [T, 32 * words] as a draft mask's words."""
+    return torch.from_numpy(np.packbits(bits.cpu().numpy(), axis=1, bitorder="little").view(np.int32).copy()).cuda()
+
+
+def tree_bits(T, words, seed):
+    return torch.rand(T, 32 * words, generator=gen(seed), device="cuda") < 0.4
+
+
+# ---- scores whose factor leaves float32's range (zero queries, zero or tiny keys)
+
+@pytest.mark.parametrize("kind", ["zero keys", "tiny keys", "all zero", "some zero queries"])
+@pytest.mark.parametrize("form", ["causal", "window", "tree"])
+@pytest.mark.parametrize("n,G,D,kv", [(40, 8, 128, 300), (70, 1, 64, 77), (33, 4, 128, 33), (300, 2, 64, 401)])
+def test_many_rows_of_zero_scores(w4, n, G, D, kv, form, kind):
+    """Zero queries and zero or tiny keys: every visible key weighs the same, hidden ones nothing."""
+    Hkv, page = 2, 16
+    g = gen(n + kv)
+    k, v = torch.randn(2, kv, Hkv, D, generator=g, device="cuda")
+    if kind != "some zero queries":
+        k *= 2.0 ** -40 if kind == "tiny keys" else 0.0
+    if kind == "all zero":
+        v *= 0
+    q = torch.randn(n, Hkv * G, D, generator=g, device="cuda").to(torch.bfloat16)
+    if kind == "some zero queries":
+        q[::3] = 0
+        k[: kv // 2] = 0                     # whole tiles of zero keys beside others
+    else:
+        q *= 0
+    pages = -(-kv // page)
+    cache = torch.full((pages, Hkv, page * (D + D // 8)), 255, dtype=torch.uint8, device="cuda")
+    slots = torch.arange(kv, device="cuda")
+    w4.w4a16_kv_append(cache, k, v, slots)
+    gk, gv = (x.double() for x in w4.w4a16_kv_read(cache, slots, D))
+    bits = tree_bits(n, -(-n // 32), 3) if form == "tree" else None
+    window = 29 if form == "window" else 0
+    lse = torch.full((n, Hkv * G), 3.0, device="cuda")
+    got = w4.w4a16_attention(q, cache, torch.arange(pages, dtype=torch.int32, device="cuda")[None], i32(kv), i32(0, n),
+                             max_q=n, scale=0.088, window=window, tree_mask=None if bits is None else packed(bits), lse=lse)
+    assert w4.w4a16_device_error() == 0
+    check(q, got, lse, reference(q, [gk], [gv], [n], [kv], float(np.float32(0.088)), True, window, bits), "bf16")
