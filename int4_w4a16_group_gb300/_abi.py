@@ -112,6 +112,25 @@ def _stream(stream) -> int:
     return stream.cuda_stream
 
 
+def _empty(shape, dtype, device, stream) -> torch.Tensor:
+    """Memory for a call on `stream` to write. The allocator hands memory out in the order of one stream's work: on
+    a stream other than the current one, a block of the current stream's could still be in use there when the call
+    writes it, and be in use by the call when the block is handed out again. Such memory comes from the call's own
+    stream, and is kept until the current stream, where the caller goes on with it, is past its last use."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    handle, current = _stream(stream), torch.cuda.current_stream()
+    if handle == current.cuda_stream:
+        return torch.empty(shape, dtype=dtype, device=device)
+    if not isinstance(stream, torch.cuda.Stream):  # (0 and 1: the legacy default stream)
+        stream = torch.cuda.ExternalStream(handle) if handle > 1 else torch.cuda.default_stream()
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    if t.is_cuda:
+        t.record_stream(current)
+    return t
+
+
 def _on_device(t, name: str) -> None:
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
@@ -328,7 +347,7 @@ def w4a16_rope_table(P: int, rot: int, base: float = 10000.0, scaling: str = "no
     if scaling not in _SCALINGS:
         raise ValueError(f"scaling: {scaling!r}, expected one of {sorted(_SCALINGS)}")
     if table is None:
-        table = torch.empty((P, rot // 2, 2), dtype=torch.float32, device="cuda")
+        table = _empty((P, rot // 2, 2), torch.float32, "cuda", stream)
     _check(_lib.w4a16_rope_table(_dev(table, torch.float32, "table", (P, rot // 2, 2)), P, rot, base,
                                  _SCALINGS[scaling], factor, original, beta_fast, beta_slow, gain,
                                  _stream(stream)), "w4a16_rope_table")
@@ -341,7 +360,7 @@ def w4a16_rope(x: torch.Tensor, positions: torch.Tensor, table: torch.Tensor, y:
     T, H, D = x.shape
     xp, xt, xh, dtype = _heads(x, "x")
     if y is None:
-        y = torch.empty((T, H, D), dtype=x.dtype, device=x.device)
+        y = _empty((T, H, D), x.dtype, x.device, stream)
         yp, yt, yh = y.data_ptr(), H * D, D
     else:
         yp, yt, yh, y_dtype = _heads(y, "y", (T, H, D))
@@ -395,9 +414,9 @@ def w4a16_kv_read(cache: torch.Tensor, slots: torch.Tensor, D: int, k: torch.Ten
     cp, pages, page_size, Hkv = _cache(cache, D)
     T = slots.shape[0]
     if k is None:
-        k = torch.empty((T, Hkv, D), dtype=torch.float32, device=cache.device)
+        k = _empty((T, Hkv, D), torch.float32, cache.device, stream)
     if v is None:
-        v = torch.empty((T, Hkv, D), dtype=torch.float32, device=cache.device)
+        v = _empty((T, Hkv, D), torch.float32, cache.device, stream)
     _check(_lib.w4a16_kv_read(cp, pages, page_size, Hkv, D, _dev(slots, torch.int64, "slots", (T,)), T,
                               _dev(k, torch.float32, "k", (T, Hkv, D)),
                               _dev(v, torch.float32, "v", (T, Hkv, D)), _stream(stream)), "w4a16_kv_read")
@@ -419,10 +438,10 @@ def w4a16_attention(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Ten
     qp, qt, qh, dtype = _heads(q, "q")
     B = kv_lens.shape[0]
     if out is None:
-        out = torch.empty((T, Hq, D), dtype=q.dtype, device=q.device)
+        out = _empty((T, Hq, D), q.dtype, q.device, stream)
     if workspace is None:
         need = w4a16_attention_workspace_size(T, B, Hkv, max(1, Hq // max(1, Hkv)), D, max_q)
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=q.device)
+        workspace = _empty(max(need, 16), torch.uint8, q.device, stream)
     _check(_lib.w4a16_attention(
         qp, qt, qh, dtype, T, Hq, cp, pages, page_size, Hkv, D,
         _dev(block_table, torch.int32, "block_table", (B, block_table.shape[1])), block_table.shape[1], B,

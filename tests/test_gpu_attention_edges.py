@@ -56,3 +56,31 @@ def test_many_rows_of_zero_scores(w4, n, G, D, kv, form, kind):
                              max_q=n, scale=0.088, window=window, tree_mask=None if bits is None else packed(bits), lse=lse)
     assert w4.w4a16_device_error() == 0
     check(q, got, lse, reference(q, [gk], [gv], [n], [kv], float(np.float32(0.088)), True, window, bits), "bf16")
+
+
+# ---- memory taken by a call on another stream
+
+@pytest.mark.parametrize("raw", [False, True])
+@pytest.mark.parametrize("n", [1, 40])
+def test_side_stream_has_memory_of_its_own(w4, n, raw):
+    """On a stream that is still busy, without workspace and out: what the current stream allocates and writes in the
+    meantime is other memory, and the call's results stay after it."""
+    cache, bt, _, _ = build_cache([3000, 700], 2, 128, 64, 4)
+    q = torch.randn(2 * n, 16, 128, generator=gen(3), device="cuda").to(torch.bfloat16)
+    args = (cache, bt, i32(3000, 700), i32(0, n, 2 * n))
+    pos, tab = torch.arange(2 * n, dtype=torch.int32, device="cuda"), w4.w4a16_rope_table(2 * n, 128)
+    slots = bt[0, :5].long() * 64
+    want = w4.w4a16_attention(q, *args, max_q=n, scale=0.1), w4.w4a16_rope(q, pos, tab), *w4.w4a16_kv_read(cache, slots, 128)
+    need = w4.w4a16_attention_workspace_size(2 * n, 2, 2, 8, 128, n)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(20_000_000)
+    on = s.cuda_stream if raw else s
+    got = (w4.w4a16_attention(q, *args, max_q=n, scale=0.1, stream=on), w4.w4a16_rope(q, pos, tab, stream=on),
+           *w4.w4a16_kv_read(cache, slots, 128, stream=on))
+    other = [torch.full((need,), 255, dtype=torch.uint8, device="cuda") for _ in range(2)]
+    torch.cuda.current_stream().wait_stream(s)
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    assert all((o == 255).all() for o in other) and w4.w4a16_device_error() == 0
