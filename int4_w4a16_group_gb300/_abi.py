@@ -169,9 +169,9 @@ def w4a16_quantize(W: torch.Tensor, qw: torch.Tensor | None = None, sc: torch.Te
     """W[K, N] float32 -> (qw[K/8, N] int32, sc[K/32, N] float32)."""
     K, N = W.shape
     if qw is None:
-        qw = torch.empty((K // 8, N), dtype=torch.int32, device=W.device)
+        qw = _empty((K // 8, N), torch.int32, W.device, stream)
     if sc is None:
-        sc = torch.empty((K // GROUP, N), dtype=torch.float32, device=W.device)
+        sc = _empty((K // GROUP, N), torch.float32, W.device, stream)
     _check(_lib.w4a16_quantize(_dev(W, torch.float32, "W"), K, N, group,
                                _dev(qw, torch.int32, "qw", (K // 8, N)),
                                _dev(sc, torch.float32, "sc", (K // GROUP, N)), _stream(stream)),
@@ -184,7 +184,7 @@ def w4a16_dequantize(qw: torch.Tensor, sc: torch.Tensor, W: torch.Tensor | None 
     K8, N = qw.shape
     K = K8 * 8
     if W is None:
-        W = torch.empty((K, N), dtype=torch.float32, device=qw.device)
+        W = _empty((K, N), torch.float32, qw.device, stream)
     _check(_lib.w4a16_dequantize(_dev(qw, torch.int32, "qw"), _dev(sc, torch.float32, "sc", (K // GROUP, N)),
                                  K, N, group, _dev(W, torch.float32, "W", (K, N)), _stream(stream)),
            "w4a16_dequantize")
@@ -197,7 +197,7 @@ def w4a16_gemm(x: torch.Tensor, qw: torch.Tensor, sc: torch.Tensor, y: torch.Ten
     M, K = x.shape
     N = qw.shape[1]
     if y is None:
-        y = torch.empty((M, N), dtype=torch.float32, device=x.device)
+        y = _empty((M, N), torch.float32, x.device, stream)
     _check(_lib.w4a16_gemm(_dev(x, torch.float32, "x"), _dev(qw, torch.int32, "qw", (K // 8, N)),
                            _dev(sc, torch.float32, "sc", (K // GROUP, N)),
                            _dev(y, torch.float32, "y", (M, N)), M, N, K, group, _stream(stream)),
@@ -211,7 +211,7 @@ def w4a16_gemm_swiglu(x: torch.Tensor, qw_gu: torch.Tensor, sc_gu: torch.Tensor,
     M, K = x.shape
     N2 = qw_gu.shape[1]
     if y is None:
-        y = torch.empty((M, N2 // 2), dtype=torch.float32, device=x.device)
+        y = _empty((M, N2 // 2), torch.float32, x.device, stream)
     _check(_lib.w4a16_gemm_swiglu(_dev(x, torch.float32, "x"),
                                   _dev(qw_gu, torch.int32, "qw_gu", (K // 8, N2)),
                                   _dev(sc_gu, torch.float32, "sc_gu", (K // GROUP, N2)),
@@ -227,7 +227,7 @@ def w4a16_gemm_bf16(x: torch.Tensor, qw: torch.Tensor, sc: torch.Tensor, y: torc
     M, K = x.shape
     N = qw.shape[1]
     if y is None:
-        y = torch.empty((M, N), dtype=torch.bfloat16, device=x.device)
+        y = _empty((M, N), torch.bfloat16, x.device, stream)
     _check(_lib.w4a16_gemm_bf16(_dev(x, torch.bfloat16, "x"), _dev(qw, torch.int32, "qw", (K // 8, N)),
                                 _dev(sc, torch.float32, "sc", (K // GROUP, N)),
                                 _dev(y, torch.bfloat16, "y", (M, N)), M, N, K, group, _stream(stream)),
@@ -247,10 +247,10 @@ def w4a16_moe_gemm(x, topk_ids, topk_w, qw_gu, sc_gu, qw_dn, sc_dn, out=None, wo
     E = qw_gu.shape[0]
     I = qw_gu.shape[2] // 2
     if out is None:
-        out = torch.empty((T, K), dtype=torch.float32, device=x.device)
+        out = _empty((T, K), torch.float32, x.device, stream)
     need = w4a16_moe_workspace_size(T, topk, E, K, I)
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=x.device)
+        workspace = _empty(max(need, 16), torch.uint8, x.device, stream)
     _check(_lib.w4a16_moe_gemm(
         _dev(x, torch.float32, "x"), _dev(topk_ids, torch.int32, "topk_ids", (T, topk)),
         _dev(topk_w, torch.float32, "topk_w", (T, topk)), T, topk, E,
@@ -277,10 +277,10 @@ def w4a16_moe_block(x, topk_ids, topk_w, qw_gu, sc_gu, qw_dn, sc_dn, qs_gu, ss_g
     I = qw_gu.shape[2] // 2
     Is = qs_gu.shape[1] // 2
     if out is None:
-        out = torch.empty((T, K), dtype=torch.float32, device=x.device)
+        out = _empty((T, K), torch.float32, x.device, stream)
     need = w4a16_moe_block_workspace_size(T, topk, E, K, I, Is)
     if workspace is None:
-        workspace = torch.empty(max(need, 16), dtype=torch.uint8, device=x.device)
+        workspace = _empty(max(need, 16), torch.uint8, x.device, stream)
     _check(_lib.w4a16_moe_block(
         _dev(x, torch.float32, "x"), _dev(topk_ids, torch.int32, "topk_ids", (T, topk)),
         _dev(topk_w, torch.float32, "topk_w", (T, topk)), T, topk, E,
@@ -306,7 +306,7 @@ def w4a16_moe_gemm_noalloc(x, topk_ids, topk_w, qw_gu, sc_gu, qw_dn, sc_dn, out=
     E = qw_gu.shape[0]
     I = qw_gu.shape[2] // 2
     if out is None:
-        out = torch.empty((T, K), dtype=torch.float32, device=x.device)
+        out = _empty((T, K), torch.float32, x.device, stream)
     _check(_lib.w4a16_moe_gemm_noalloc(
         _dev(x, torch.float32, "x"), _dev(topk_ids, torch.int32, "topk_ids", (T, topk)),
         _dev(topk_w, torch.float32, "topk_w", (T, topk)), T, topk, E,
@@ -457,7 +457,7 @@ def w4a16_attention(q: torch.Tensor, cache: torch.Tensor, block_table: torch.Ten
 def w4a16_topk_softmax(logits: torch.Tensor, weights: torch.Tensor | None = None, stream=None):
     T, topk = logits.shape
     if weights is None:
-        weights = torch.empty_like(logits)
+        weights = _empty((T, topk), logits.dtype, logits.device, stream)
     _check(_lib.w4a16_topk_softmax(_dev(logits, torch.float32, "logits"),
                                    _dev(weights, torch.float32, "weights", (T, topk)), T, topk,
                                    _stream(stream)),
@@ -541,7 +541,7 @@ class Registry:
         K, N = self.find(name)
         M = x.shape[0]
         if y is None:
-            y = torch.empty((M, N), dtype=torch.float32, device=x.device)
+            y = _empty((M, N), torch.float32, x.device, stream)
         _check(_lib.w4a16_linear(self._h, name.encode(), _dev(x, torch.float32, "x", (M, K)),
                                  _dev(y, torch.float32, "y", (M, N)), M, _stream(stream)),
                f"w4a16_linear({name})")
@@ -551,7 +551,7 @@ class Registry:
         K, N = self.find(name)
         M = x.shape[0]
         if y is None:
-            y = torch.empty((M, N // 2), dtype=torch.float32, device=x.device)
+            y = _empty((M, N // 2), torch.float32, x.device, stream)
         _check(_lib.w4a16_linear_swiglu(self._h, name.encode(), _dev(x, torch.float32, "x", (M, K)),
                                         _dev(y, torch.float32, "y", (M, N // 2)), M, _stream(stream)),
                f"w4a16_linear_swiglu({name})")

@@ -50,7 +50,7 @@ def abi(monkeypatch):
 
     class Lib:
         def __getattr__(self, name):
-            return (lambda *a: 1 << 10) if name.endswith("_size") else (lambda *a: 0)
+            return (lambda *a: 1 << 10) if name.endswith(("_size", "_create")) else (lambda *a: 0)
 
     monkeypatch.setattr(_abi, "_lib", Lib())
     monkeypatch.setattr(_abi, "_device", lambda: 0)
@@ -93,3 +93,38 @@ def check_calls(abi, calls):
 
 def test_attention_entries(abi):
     check_calls(abi, attention_calls)
+
+
+def linear_calls(a):
+    i32, u = torch.int32, torch.float32
+    K, N, T, E = 64, 64, 3, 2
+    x, qw, sc = on_gpu(T, K), on_gpu(K // 8, N, dtype=i32), on_gpu(K // 32, N)
+    ids, w = on_gpu(T, 2, dtype=i32), on_gpu(T, 2)
+    gu, dn = (on_gpu(E, K // 8, N, dtype=i32), on_gpu(E, K // 32, N)), (on_gpu(E, 4, K, dtype=i32), on_gpu(E, 1, K))
+    shared = (qw, sc, on_gpu(4, K, dtype=i32), on_gpu(1, K))
+    return {
+        "quantize": (2, lambda s: a.w4a16_quantize(on_gpu(K, N, dtype=u), stream=s)),
+        "dequantize": (1, lambda s: a.w4a16_dequantize(qw, sc, stream=s)),
+        "gemm": (1, lambda s: a.w4a16_gemm(x, qw, sc, stream=s)),
+        "gemm_swiglu": (1, lambda s: a.w4a16_gemm_swiglu(x, qw, sc, stream=s)),
+        "gemm_bf16": (1, lambda s: a.w4a16_gemm_bf16(on_gpu(T, K, dtype=torch.bfloat16), qw, sc, stream=s)),
+        "moe_gemm": (2, lambda s: a.w4a16_moe_gemm(x, ids, w, *gu, *dn, stream=s)),
+        "moe_block": (2, lambda s: a.w4a16_moe_block(x, ids, w, *gu, *dn, *shared, stream=s)),
+        "moe_gemm_noalloc": (1, lambda s: a.w4a16_moe_gemm_noalloc(x, ids, w, *gu, *dn, stream=s)),
+        "topk_softmax": (1, lambda s: a.w4a16_topk_softmax(w, stream=s)),
+    }
+
+
+def test_linear_and_moe_entries(abi):
+    check_calls(abi, linear_calls)
+
+
+def test_registry_entries(abi, monkeypatch):
+    a, _ = abi
+    monkeypatch.setattr(a.Registry, "find", lambda self, name: (64, 64))
+    r, x = a.Registry(), on_gpu(3, 64)
+    try:
+        check_calls(abi, lambda a: {"linear": (1, lambda s: r.linear("w", x, stream=s)),
+                                    "linear_swiglu": (1, lambda s: r.linear_swiglu("w", x, stream=s))})
+    finally:
+        r.close()           # its handle is not the library's
