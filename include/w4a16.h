@@ -311,7 +311,8 @@ w4a16_status w4a16_kv_read(const void* cache, int num_pages, int page_size, int 
  * 0 to T) and kv_lens[b] cached tokens, token j on page block_table[b, j / page_size] (int32
  * [B, max_pages]). Query token i of n stands at position kv_lens[b] - n + i.
  *   causal      it sees the keys up to its own position (0: all kv_lens[b] keys);
- *   window      with causal: only the last `window` of those (0: no window);
+ *   window      with causal: only the last `window` of those (0: no window); keys before every row's
+ *               window are not looked at: their pages may be gone from block_table;
  *   tree_mask   [T, mask_words] or NULL: draft tokens of a tree. It sees every key before the
  *               sequence's n draft tokens, and draft token d if bit d % 32 of word d / 32 of its row
  *               is set (drafts past the row's words are not seen). Not with a window; causal is 1.

@@ -199,7 +199,7 @@ struct Walk {
   unsigned int* err;
   int b = -1, h = 0, rt = 0;                 // position
   KvSeq s = {0, 0, 0};                       // sequence b
-  int lo_aligned = 0, hi = 0, tiles = 0;     // of row tile rt
+  int lo = 0, hi = 0, tiles = 0;             // of row tile rt: keys [lo, hi) that any of its rows may see
   long long tile0 = 0;                       // place of the item's tile 0 on the line
 
   __device__ Walk(const AttnArgs& a_, int page_size, int max_rows_, int min_rows_, int Hkv_, unsigned int* err_)
@@ -223,12 +223,14 @@ struct Walk {
   __device__ int row_tiles(const KvSeq& q) const { return (q.n * a.G + R - 1) / R; }
   __device__ void range(const KvSeq& q, int r, int* lo, int* end) const {
     const int i0 = r * R / a.G, i1 = (min((r + 1) * R, q.n * a.G) - 1) / a.G;
-    *lo = kv_lo(q, i0, a.window) / tile_keys * tile_keys;
+    *lo = kv_lo(q, i0, a.window);
     *end = kv_hi(q, i1, a.causal, a.mask != nullptr);
   }
+  static __device__ int first_key(int lo) { return lo & -tile_keys; }  // of tile 0
   __device__ int tiles_of(const KvSeq& q, int r) const {
     int lo, end;
     range(q, r, &lo, &end);
+    lo = first_key(lo);
     return end > lo ? (end - lo + tile_keys - 1) / tile_keys : 1;
   }
   __device__ long long head_units(const KvSeq& q) const {
@@ -292,7 +294,7 @@ struct Walk {
       ++rt;
     }
     tile0 = u + cost;
-    range(s, rt, &lo_aligned, &hi);
+    range(s, rt, &lo, &hi);
   }
   // To the item after this one (there is one).
   __device__ void next_item() {
@@ -306,7 +308,7 @@ struct Walk {
       }
     }
     tiles = tiles_of(s, rt);
-    range(s, rt, &lo_aligned, &hi);
+    range(s, rt, &lo, &hi);
   }
   // Tile of the item at or after place `at`.
   __device__ int tile_at(long long at) const {

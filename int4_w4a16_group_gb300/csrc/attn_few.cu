@@ -108,14 +108,14 @@ __global__ void __launch_bounds__(kWarps * 32, NG <= 4 && NB == 1 && sizeof(T) =
     }
     const int rows = min(R, sq.n * a.G - w.rt * R);
     const int r0 = w.rt * R;              // first row of the item: row = token * G + head
-    const int key0 = w.lo_aligned;        // first key of tile 0
+    const int key0 = w.first_key(w.lo);   // first key of tile 0
     const int i_first = r0 / a.G, i_last = (r0 + rows - 1) / a.G;
     const bool masked = a.mask != nullptr;
     const int dbase = sq.len - sq.n;      // first draft key
     // keys that every row of the item sees
     const int full_hi = masked ? dbase : kv_hi(sq, i_first, a.causal, false);
     const int full_lo = kv_lo(sq, i_last, a.window);
-    const int key_end = w.hi;
+    const int key_lo = w.lo, key_end = w.hi;  // (blocks wholly outside are not looked at)
 
     // ---- the ring: tiles t_begin + warp + 4 k of this warp
     const int* bt = a.block_table + (size_t)w.b * a.max_pages;
@@ -123,13 +123,13 @@ __global__ void __launch_bounds__(kWarps * 32, NG <= 4 && NB == 1 && sizeof(T) =
     // page of lane's block (lane 0, 1) of a tile, or -1
     auto page_id = [&](int tile) {
       const int key = key0 + tile * kTile + (lane & 1) * kKvBlock;
-      return (lane < 2 && tile < t_end && key < key_end) ? __ldg(bt + (key >> page_shift)) : -1;
+      return (lane < 2 && tile < t_end && key + kKvBlock > key_lo && key < key_end) ? __ldg(bt + (key >> page_shift)) : -1;
     };
     uint32_t valid = 0;  // two bits per stage: the tile's blocks that were copied
     auto issue = [&](int tile, int stage, int page) {
       if (failed || tile >= t_end) return;
       const int key = key0 + tile * kTile + (lane & 1) * kKvBlock;
-      const bool want = lane < 2 && key < key_end;
+      const bool want = lane < 2 && key + kKvBlock > key_lo && key < key_end;
       const bool ok = want && page >= 0 && page < c.num_pages;
       const uint32_t okm = __ballot_sync(0xFFFFFFFFu, ok);
       if (__any_sync(0xFFFFFFFFu, want && !ok) && lane == 0 && err) atomicCAS(err, 0u, 1u);
@@ -313,7 +313,7 @@ __global__ void __launch_bounds__(kWarps * 32, NG <= 4 && NB == 1 && sizeof(T) =
 #pragma unroll
           for (int hf = 0; hf < 2; ++hf) {
             const int key = kbase + blk * 16 + hf * 8 + kkey;
-            const bool there = ((okm >> blk) & 1u) && key < key_end;
+            const bool there = ((okm >> blk) & 1u) && key >= key_lo && key < key_end;
             if (!there) {  // whatever the bytes are, they take no part
 #pragma unroll
               for (int k = 0; k < NG / 2; ++k) vs[blk][hf][k] = 0u;

@@ -349,10 +349,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     int ve = 0;          // item's running V exponent field
     bool wrote = false;  // this lane changed scales since the last copy
     uint32_t pend_ok[2] = {0, 0};  // of the two tiles issued last: blocks copied,
-    int pend_keys[2] = {0, 0};     // visible keys,
+    int pend_lo[2] = {0, 0}, pend_keys[2] = {0, 0};  // its keys [lo, keys) that rows may see,
     int pend_flags[2] = {0, 0};
     bool ok = true;
-    auto look = [&](int i, uint32_t copied, int keys, int flags) {
+    auto look = [&](int i, uint32_t copied, int lo, int keys, int flags) {
       const int s = i % kRawStages;
       if (!wait_warp(kRawFull + s, (i / kRawStages) & 1)) return false;
       const uint32_t st = sb + L::raw + s * L::raw_tile;
@@ -363,7 +363,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t ks[NG / 2], vs[NG / 2];
         lds_words<NG / 2>(st + blk * L::block + kv_scales_off(D, 0) + r * NG * 2, ks);
         lds_words<NG / 2>(st + blk * L::block + kv_scales_off(D, 1) + r * NG * 2, vs);
-        if (((copied >> blk) & 1u) && key < keys) {
+        if (((copied >> blk) & 1u) && key >= lo && key < keys) {
 #pragma unroll
           for (int k = 0; k < NG / 2; ++k) {
             mk = __vmaxu2(mk, ks[k] & 0x7FFF7FFFu);
@@ -392,24 +392,24 @@ __global__ void __launch_bounds__(kThreads, 1)
     // Step n issues tile n and looks at tile n - 2; two more steps after the last tile.
     int t = w.tile_at(begin), t1 = w.tile_at(end), after = 0;
     auto page_of = [&](int tile) {
-      const int key = w.lo_aligned + tile * kKeys + lane * kKvBlock;
-      return lane < kKeys / kKvBlock && tile < t1 && key < w.hi
+      const int key = w.first_key(w.lo) + tile * kKeys + lane * kKvBlock;
+      return lane < kKeys / kKvBlock && tile < t1 && key + kKvBlock > w.lo && key < w.hi
                  ? __ldg(a.block_table + (size_t)w.b * a.max_pages + (key >> page_shift)) : -1;
     };
     int next_page = page_of(t), steps = 0;
     bool first = true;
     for (;; ++steps) {
-      if (steps > 1 && !look(steps - 2, pend_ok[1], pend_keys[1], pend_flags[1])) {
+      if (steps > 1 && !look(steps - 2, pend_ok[1], pend_lo[1], pend_keys[1], pend_flags[1])) {
         ok = false;
         break;
       }
-      pend_ok[1] = pend_ok[0], pend_keys[1] = pend_keys[0], pend_flags[1] = pend_flags[0];
+      pend_ok[1] = pend_ok[0], pend_lo[1] = pend_lo[0], pend_keys[1] = pend_keys[0], pend_flags[1] = pend_flags[0];
       if (after) {  // no tile left to issue
         if (++after == 3) break;
         continue;
       }
-      const int base = w.lo_aligned + t * kKeys, key = base + lane * kKvBlock;
-      const bool want = lane < kKeys / kKvBlock && key < w.hi;
+      const int base = w.first_key(w.lo) + t * kKeys, key = base + lane * kKvBlock;
+      const bool want = lane < kKeys / kKvBlock && key + kKvBlock > w.lo && key < w.hi;
       const int page = next_page;
       const bool good = want && page >= 0 && page < c.num_pages;
       const uint32_t okm = __ballot_sync(0xFFFFFFFFu, good);
@@ -431,7 +431,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++n;
       const bool item_ends = t + 1 == t1, run_ends = item_ends && w.tile0 + w.tiles + kManyItemCost >= end;
       pend_ok[0] = okm;
-      pend_keys[0] = w.hi - base;
+      pend_lo[0] = w.lo - base, pend_keys[0] = w.hi - base;
       pend_flags[0] = (first ? kFirst : 0) | (item_ends ? kLast : 0) | (run_ends ? kEnd : 0) |
                       (w.s.n * a.G - w.rt * 2 * kRows > kRows ? kBoth : 0);
       first = item_ends;
@@ -759,7 +759,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           tc::fence_after();
           const TileInfo ti = info[n % kInfos];
-          const int kbase = w.lo_aligned + t * kKeys;
+          const int kbase = w.first_key(w.lo) + t * kKeys;
           const bool full = ti.there == (1u << (kKeys / kKvBlock)) - 1u && kbase + kKeys <= min(full_hi, key_end) &&
                             kbase >= full_lo;
           uint32_t vis[4] = {0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu, 0xFFFFFFFFu};

@@ -84,3 +84,49 @@ def test_side_stream_has_memory_of_its_own(w4, n, raw):
     for a, b in zip(got, want):
         assert torch.equal(a, b)
     assert all((o == 255).all() for o in other) and w4.w4a16_device_error() == 0
+
+
+# ---- what the cache and the block table hold at keys that no row sees
+
+def poison(cache, bt, page, D, b, keys, scale_bits):
+    """Codes of all ones and the given bf16 scale bits at the places of a sequence's keys."""
+    blocks = cache.view(cache.shape[0], cache.shape[1], page // 16, -1)
+    at = (bt[b].long()[keys // page][:, None], torch.arange(cache.shape[1], device="cuda")[None],
+          (keys % page // 16)[:, None], (keys % 16)[:, None])
+    for part in (0, 1):
+        blocks[..., part * 8 * D:(part + 1) * 8 * D].unflatten(-1, (16, D // 2))[at] = 255
+        scales = blocks[..., 16 * D + part * D:16 * D + (part + 1) * D].unflatten(-1, (16, D // 16))
+        scales[at] = torch.tensor([scale_bits & 255, scale_bits >> 8] * (D // 32), dtype=torch.uint8, device="cuda")
+
+
+JUNK = [0xFFFF, 0x7F80, 0x7F00, 0x5F00]   # NaN, infinity, 2^127, 2^63
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("seqs,Hkv,G,D,page,window", [
+    ([(1, 2000), (1, 40)], 2, 8, 128, 16, 50), ([(1, 333)], 1, 4, 64, 64, 1), ([(1, 700)], 1, 5, 256, 32, 33),
+    ([(40, 1500), (3, 200)], 2, 8, 128, 16, 100), ([(70, 900)], 1, 2, 64, 16, 7), ([(300, 1111)], 1, 4, 128, 32, 130),
+    ([(9, 129), (33, 257)], 2, 16, 64, 16, 1),
+])
+def test_nothing_behind_the_window_is_looked_at(w4, seqs, Hkv, G, D, page, window, dtype):
+    """Pages wholly behind every row's window may be gone from the block table, and hidden tokens of the page at
+    the border may be anything."""
+    ns, kvs = [s[0] for s in seqs], [s[1] for s in seqs]
+    cache, bt, keys, values = build_cache(kvs, Hkv, D, page, 5)
+    q = torch.randn(sum(ns), Hkv * G, D, generator=gen(8), device="cuda").to(DT[dtype])
+    starts = i32(0, *np.cumsum(ns).tolist())
+    kw = dict(max_q=max(ns), scale=0.1, window=window)
+    lse = torch.empty(sum(ns), Hkv * G, device="cuda")
+    want = w4.w4a16_attention(q, cache, bt, i32(*kvs), starts, lse=lse, **kw)
+    check(q, want, lse, reference(q, keys, values, ns, kvs, float(np.float32(0.1)), True, window, None), dtype)
+    for junk in JUNK:
+        bad, table = cache.clone(), bt.clone()
+        for b, (n, kv) in enumerate(seqs):
+            lo = max(0, kv - n + 1 - window)
+            poison(bad, bt, page, D, b, torch.arange(lo, device="cuda"), junk)
+            # gone, or (every other page) an entry that was never written
+            table[b, :lo // page] = -1
+            table[b, 1:lo // page:2] = bt[b, 1:lo // page:2]
+        got = w4.w4a16_attention(q, bad, table, i32(*kvs), starts, **kw)
+        assert w4.w4a16_device_error() == 0
+        assert torch.equal(got, want)
