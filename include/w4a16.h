@@ -316,6 +316,7 @@ w4a16_status w4a16_kv_read(const void* cache, int num_pages, int page_size, int 
  *   tree_mask   [T, mask_words] or NULL: draft tokens of a tree. It sees every key before the
  *               sequence's n draft tokens, and draft token d if bit d % 32 of word d / 32 of its row
  *               is set (drafts past the row's words are not seen). Not with a window; causal is 1.
+ *               A draft that no row sees takes no part, whatever the cache holds at its place.
  * A row that sees no key is zero with lse = -inf. lse [T, Hq] (or NULL) receives
  * ln sum_j exp(scale * q . K[j]). out is [T, Hq, D] contiguous, of q's type.
  * max_q is an upper bound of the sequences' query tokens, known to the host; rows of a sequence with

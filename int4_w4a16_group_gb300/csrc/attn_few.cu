@@ -314,10 +314,7 @@ __global__ void __launch_bounds__(kWarps * 32, NG <= 4 && NB == 1 && sizeof(T) =
           for (int hf = 0; hf < 2; ++hf) {
             const int key = kbase + blk * 16 + hf * 8 + kkey;
             const bool there = ((okm >> blk) & 1u) && key >= key_lo && key < key_end;
-            if (!there) {  // whatever the bytes are, they take no part
-#pragma unroll
-              for (int k = 0; k < NG / 2; ++k) vs[blk][hf][k] = 0u;
-            }
+            bool seen = false;  // by a row of the lane's columns
 #pragma unroll
             for (int nb = 0; nb < NB; ++nb)
 #pragma unroll
@@ -327,7 +324,14 @@ __global__ void __launch_bounds__(kWarps * 32, NG <= 4 && NB == 1 && sizeof(T) =
                            key >= kv_lo(sq, i, a.window);
                 if (see && masked && key >= dbase) see = draft_bit(a, sq.q0 + i, key - dbase);
                 if (!see) sc[blk][nb][2 * hf + k] = -CUDART_INF_F;
+                seen = seen || see;
               }
+            // whatever the bytes of a key are that no row sees, they take no part
+            const uint32_t lanes = __ballot_sync(0xFFFFFFFFu, seen);
+            if (!((lanes >> (lane & 28)) & 15u)) {
+#pragma unroll
+              for (int k = 0; k < NG / 2; ++k) vs[blk][hf][k] = 0u;
+            }
           }
       }
       bool grow = false;

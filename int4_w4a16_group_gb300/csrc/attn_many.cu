@@ -349,10 +349,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     int ve = 0;          // item's running V exponent field
     bool wrote = false;  // this lane changed scales since the last copy
     uint32_t pend_ok[2] = {0, 0};  // of the two tiles issued last: blocks copied,
-    int pend_lo[2] = {0, 0}, pend_keys[2] = {0, 0};  // its keys [lo, keys) that rows may see,
+    uint32_t pend_seen[2] = {0, 0};  // its keys that a row of the item sees (lane q: keys 32 (q % 4) ..),
     int pend_flags[2] = {0, 0};
     bool ok = true;
-    auto look = [&](int i, uint32_t copied, int lo, int keys, int flags) {
+    auto look = [&](int i, uint32_t copied, uint32_t seen, int flags) {
       const int s = i % kRawStages;
       if (!wait_warp(kRawFull + s, (i / kRawStages) & 1)) return false;
       const uint32_t st = sb + L::raw + s * L::raw_tile;
@@ -363,14 +363,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint32_t ks[NG / 2], vs[NG / 2];
         lds_words<NG / 2>(st + blk * L::block + kv_scales_off(D, 0) + r * NG * 2, ks);
         lds_words<NG / 2>(st + blk * L::block + kv_scales_off(D, 1) + r * NG * 2, vs);
-        if (((copied >> blk) & 1u) && key >= lo && key < keys) {
+        if ((__shfl_sync(0xFFFFFFFFu, seen, p) >> lane) & 1u) {
 #pragma unroll
           for (int k = 0; k < NG / 2; ++k) {
             mk = __vmaxu2(mk, ks[k] & 0x7FFF7FFFu);
             mv = __vmaxu2(mv, vs[k] & 0x7FFF7FFFu);
           }
         } else {
-          wrote = true;  // whatever the bytes are: K' and V' of keys that are not there are zeros
+          wrote = true;  // whatever the bytes are: K' and V' of keys that no row sees are zeros
 #pragma unroll
           for (int k = 0; k < NG / 2; ++k) {
             sts32(st + blk * L::block + kv_scales_off(D, 0) + r * NG * 2 + 4 * k, 0u);
@@ -399,11 +399,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     int next_page = page_of(t), steps = 0;
     bool first = true;
     for (;; ++steps) {
-      if (steps > 1 && !look(steps - 2, pend_ok[1], pend_lo[1], pend_keys[1], pend_flags[1])) {
+      if (steps > 1 && !look(steps - 2, pend_ok[1], pend_seen[1], pend_flags[1])) {
         ok = false;
         break;
       }
-      pend_ok[1] = pend_ok[0], pend_lo[1] = pend_lo[0], pend_keys[1] = pend_keys[0], pend_flags[1] = pend_flags[0];
+      pend_ok[1] = pend_ok[0], pend_seen[1] = pend_seen[0], pend_flags[1] = pend_flags[0];
       if (after) {  // no tile left to issue
         if (++after == 3) break;
         continue;
@@ -431,7 +431,21 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++n;
       const bool item_ends = t + 1 == t1, run_ends = item_ends && w.tile0 + w.tiles + kManyItemCost >= end;
       pend_ok[0] = okm;
-      pend_lo[0] = w.lo - base, pend_keys[0] = w.hi - base;
+      const int k0 = base + 32 * (lane & 3);
+      uint32_t seen = bit_range(w.lo - k0, w.hi - k0) & ((okm >> (2 * (lane & 3)) & 1u ? 0x0000FFFFu : 0u) |
+                                                         (okm >> (2 * (lane & 3)) & 2u ? 0xFFFF0000u : 0u));
+      const int dbase = w.s.len - w.s.n;
+      if (a.mask != nullptr && base + kKeys > dbase) {  // drafts: those that the mask shows to one of the item's tokens
+        const int r0 = w.rt * 2 * kRows, i_last = (min(r0 + 2 * kRows, w.s.n * a.G) - 1) / a.G;
+        uint32_t any = 0;
+#pragma unroll 4
+        for (int i = r0 / a.G + (lane >> 2); i <= i_last; i += 8) any |= draft_bits(a, w.s.q0 + i, k0 - dbase);
+        any |= __shfl_xor_sync(0xFFFFFFFFu, any, 4);
+        any |= __shfl_xor_sync(0xFFFFFFFFu, any, 8);
+        any |= __shfl_xor_sync(0xFFFFFFFFu, any, 16);
+        seen &= any;
+      }
+      pend_seen[0] = seen;
       pend_flags[0] = (first ? kFirst : 0) | (item_ends ? kLast : 0) | (run_ends ? kEnd : 0) |
                       (w.s.n * a.G - w.rt * 2 * kRows > kRows ? kBoth : 0);
       first = item_ends;

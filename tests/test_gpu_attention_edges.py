@@ -130,3 +130,34 @@ def test_nothing_behind_the_window_is_looked_at(w4, seqs, Hkv, G, D, page, windo
         got = w4.w4a16_attention(q, bad, table, i32(*kvs), starts, **kw)
         assert w4.w4a16_device_error() == 0
         assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("seqs,Hkv,G,D,page,real", [
+    ([(16, 900), (16, 16), (16, 333)], 2, 8, 128, 32, 7), ([(2, 40)], 1, 4, 64, 16, 1), ([(64, 500)], 1, 8, 128, 64, 33),
+    ([(100, 130)], 1, 1, 64, 16, 40), ([(40, 300), (5, 90)], 1, 2, 256, 32, 3), ([(150, 700)], 2, 4, 128, 16, 100),
+    ([(40, 30)], 1, 8, 128, 16, 20),
+])
+def test_drafts_that_no_row_sees(w4, seqs, Hkv, G, D, page, real, dtype):
+    """A tree padded to a fixed size: the places of drafts that no row's mask shows may be anything."""
+    ns, kvs = [s[0] for s in seqs], [s[1] for s in seqs]
+    T, words = sum(ns), -(-max(ns) // 32)
+    cache, bt, keys, values = build_cache(kvs, Hkv, D, page, 5)
+    q = torch.randn(T, Hkv * G, D, generator=gen(8), device="cuda").to(DT[dtype])
+    starts = i32(0, *np.cumsum(ns).tolist())
+    bits = tree_bits(T, words, 4)
+    bits[:, real:] = False                  # drafts from `real` on are padding,
+    bits[:, real // 2] = False              # and one in the middle is seen by nobody
+    kw = dict(max_q=max(ns), scale=0.1, tree_mask=packed(bits))
+    lse = torch.empty(T, Hkv * G, device="cuda")
+    want = w4.w4a16_attention(q, cache, bt, i32(*kvs), starts, lse=lse, **kw)
+    check(q, want, lse, reference(q, keys, values, ns, kvs, float(np.float32(0.1)), True, 0, bits), dtype)
+    for junk in JUNK:
+        bad = cache.clone()
+        for b, (n, kv) in enumerate(seqs):
+            d = torch.arange(n, device="cuda")
+            d = d[((d >= real) | (d == real // 2)) & (kv - n + d >= 0)]
+            poison(bad, bt, page, D, b, kv - n + d, junk)
+        got = w4.w4a16_attention(q, bad, bt, i32(*kvs), starts, **kw)
+        assert w4.w4a16_device_error() == 0
+        assert torch.equal(got, want)
