@@ -70,8 +70,8 @@ W4A16_HD int kv_hi(const KvSeq& s, int i, int causal, bool masked) {
 }
 W4A16_HD int kv_lo(const KvSeq& s, int i, int window) {
   if (window <= 0) return 0;
-  const int p = s.len - s.n + i + 1 - window;
-  return p < 0 ? 0 : p;
+  const int p = s.len - s.n + i + 1;
+  return p <= window ? 0 : p - window;  // (p - window first would overflow for p < 0 and the largest windows)
 }
 
 }  // namespace w4a16

@@ -161,3 +161,19 @@ def test_drafts_that_no_row_sees(w4, seqs, Hkv, G, D, page, real, dtype):
         got = w4.w4a16_attention(q, bad, bt, i32(*kvs), starts, **kw)
         assert w4.w4a16_device_error() == 0
         assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n,kv", [(40, 3), (300, 120), (5, 2), (1, 50)])
+def test_largest_window_is_no_window(w4, n, kv, dtype):
+    """The largest window an int holds, also where query tokens stand before the first key."""
+    cache, bt, keys, values = build_cache([kv], 1, 128, 16, 5)
+    q = torch.randn(n, 8, 128, generator=gen(8), device="cuda").to(DT[dtype])
+    args = (q, cache, bt, i32(kv), i32(0, n))
+    lse, lse2 = torch.empty(2, n, 8, device="cuda")
+    want = w4.w4a16_attention(*args, max_q=n, scale=0.1, lse=lse)
+    check(q, want, lse, reference(q, keys, values, [n], [kv], float(np.float32(0.1)), True, 0, None), dtype)
+    for window in (2 ** 31 - 1, 2 ** 31 - n, 2 ** 30):
+        got = w4.w4a16_attention(*args, max_q=n, scale=0.1, window=window, lse=lse2)
+        assert torch.equal(got, want) and torch.equal(lse, lse2)
+    assert w4.w4a16_device_error() == 0
