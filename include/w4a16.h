@@ -269,7 +269,8 @@ w4a16_status w4a16_rope_table(float* table, int P, int rot, double base, int sca
  * (a, b) -> (a cos - b sin, b cos + a sin), pairs (i, i + rot/2), or (2i, 2i + 1) if `interleaved`;
  * `inverse` turns the other way. Computed in float32, rounded once. D a multiple of 8, rot even and
  * at most D. positions [T] int32 in [0, P): a token outside is copied unturned and flagged. y may be
- * x itself (same strides), and may not overlap it otherwise. */
+ * x itself (same strides), and may not overlap it otherwise; its heads may not overlap each other
+ * (W4A16_ERR_ARG). */
 w4a16_status w4a16_rope(const void* x, int64_t x_token, int64_t x_head, int dtype, int T, int H,
                         int D, const int32_t* positions, const float* table, int P, int rot,
                         int interleaved, int inverse, void* y, int64_t y_token, int64_t y_head,

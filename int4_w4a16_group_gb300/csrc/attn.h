@@ -5,12 +5,9 @@
 #include <stddef.h>
 #include <stdint.h>
 
-namespace w4a16 {
+#include "heads.h"
 
-// Strides in elements of a [tokens, heads, D] tensor whose last dimension is contiguous.
-struct HeadStrides {
-  long long token, head;
-};
+namespace w4a16 {
 
 struct RopeTableArgs {
   int P, rot, scaling, original;

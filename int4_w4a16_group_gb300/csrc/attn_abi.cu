@@ -72,6 +72,7 @@ w4a16_status w4a16_rope(const void* x, int64_t x_token, int64_t x_head, int dtyp
   if (!strides_ok(dtype, x_token, x_head) || !strides_ok(dtype, y_token, y_head))
     return W4A16_ERR_ALIGN;
   if (x == y && (x_token != y_token || x_head != y_head)) return W4A16_ERR_ARG;
+  if (!heads_disjoint(T, H, {y_token, y_head}, D)) return W4A16_ERR_ARG;
   const RopeArgs r = {positions, table, P, rot, interleaved ? 1 : 0};
   return cuda_status(launch_rope(x, {x_token, x_head}, y, {y_token, y_head}, dtype == W4A16_BF16,
                                  T, H, D, r, inverse != 0, (cudaStream_t)stream));

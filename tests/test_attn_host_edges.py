@@ -44,3 +44,71 @@ def test_borders_of_any_window(tmp_path):
                     str(src), "-o", str(exe)], check=True, capture_output=True)
     r = subprocess.run([str(exe)], capture_output=True, text=True)
     assert r.returncode == 0, r.stderr
+
+
+@pytest.fixture(scope="module")
+def lib():
+    from int4_w4a16_group_gb300.build import build
+    build()
+    import int4_w4a16_group_gb300 as w4
+    return w4.C
+
+
+# ------------------------------------------------------------------------------------- overlapping heads
+
+OVERLAP = r"""
+#include <cstdio>
+#include <cstdlib>
+#include "heads.h"
+using namespace w4a16;
+int main() {
+  int counts[2] = {0, 0};
+  for (int D : {8, 72})
+    for (int T : {1, 2, 3, 5})
+      for (int H : {1, 2, 3, 4, 9})
+        for (int a = -6; a <= 9; ++a)
+          for (int b = -6; b <= 9; ++b)
+            for (int odd : {0, -4}) {
+              const long long token = a * D + odd, head = b * D / 2;
+              bool apart = true;
+              for (int i = 0; i < T * H; ++i)
+                for (int j = 0; j < i; ++j) {
+                  const long long d = (i / H - j / H) * token + (i % H - j % H) * head;
+                  if (llabs(d) < D) apart = false;
+                }
+              if (heads_disjoint(T, H, {token, head}, D) != apart) {
+                printf("T %d H %d D %d token %lld head %lld\n", T, H, D, token, head);
+                return 1;
+              }
+              ++counts[apart];
+            }
+  // strides whose products pass 64 bits
+  const long long big = (1ll << 62);
+  if (!heads_disjoint(3, 5, {big, 128}, 128) || !heads_disjoint(3, 5, {128, big}, 128)) return 2;
+  if (!heads_disjoint(3, 5, {-big, big - 128}, 128) || heads_disjoint(3, 5, {-big, big - 64}, 128)) return 3;
+  return counts[0] > 100 && counts[1] > 100 ? 0 : 4;
+}
+"""
+
+
+@pytest.mark.skipif(shutil.which("g++") is None, reason="needs g++")
+def test_overlap_of_strided_heads(tmp_path):
+    """Against every pair of heads, for strides of either sign and order."""
+    src, exe = tmp_path / "overlap.cpp", tmp_path / "overlap"
+    src.write_text("#include <initializer_list>\n" + OVERLAP)
+    subprocess.run(["g++", "-std=c++17", "-O1", "-Wall", "-I", CSRC, str(src), "-o", str(exe)], check=True,
+                   capture_output=True)
+    r = subprocess.run([str(exe)], capture_output=True, text=True)
+    assert r.returncode == 0, r.stdout
+
+
+X, P, Y = 0x10000, 0x20000, 0x30000   # fake, aligned: the check must fail before any use
+
+
+@pytest.mark.parametrize("T,token,H,head,D", [
+    (4, 0, 8, 128, 128), (4, 1024, 8, 0, 128), (2, 1016, 8, 128, 128), (4, 1024, 8, 120, 128), (5, 128, 8, 512, 128),
+    (4, 120, 2, 4096, 128), (5, 384, 4, 512, 128),
+])
+def test_rope_refuses_outputs_that_overlap(lib, T, token, H, head, D):
+    for dtype in (0, 1):
+        assert lib.w4a16_rope(X, H * D, D, dtype, T, H, D, P, P, 16, 8, 0, 0, Y, token, head, None) == 1
