@@ -175,7 +175,8 @@ enum RopeMode { kPairs, kHalvesVec, kHalvesScalar };
 // A thread owns one slot of the head -- a 16-byte vector (pairs side by side), two vectors rot/2
 // apart (halves), or one pair or element where rot/2 is no whole number of vectors -- for kHeads
 // heads of a token, so the table's entries are read once for kHeads rotations and kHeads loads are
-// in flight. Every element is read and written by the same thread, so y may be x.
+// in flight. Every element is read and written by the same thread, so y may be x. What is only copied goes
+// through no arithmetic: a turn by (1, 0) would make infinity's partner NaN and lose the sign of zeros.
 constexpr int kHeads = 4;
 
 template <typename T, RopeMode MODE>
@@ -211,7 +212,7 @@ __global__ void __launch_bounds__(256)
       for (int h = 0; h < kHeads && h0 + h < H; ++h) {
         if (slot < half) {
           float a = to_f(xp[h * xs.head + d]), b = to_f(xp[h * xs.head + d + half]);
-          turn(a, b, cs, sign);
+          if (rotate) turn(a, b, cs, sign);
           yp[h * ys.head + d] = from_f<T>(a);
           yp[h * ys.head + d + half] = from_f<T>(b);
         } else {
@@ -235,7 +236,8 @@ __global__ void __launch_bounds__(256)
         for (int h = 0; h < kHeads; ++h)
           if (h0 + h < H) {
 #pragma unroll
-            for (int j = 0; j < N; ++j) turn(a[h].v[j], b[h].v[j], cs[j], sign);
+            for (int j = 0; j < N; ++j)
+              if (rotate) turn(a[h].v[j], b[h].v[j], cs[j], sign);
             a[h].store(yp + h * ys.head + d);
             b[h].store(yp + h * ys.head + d + half);
           }
@@ -263,7 +265,8 @@ __global__ void __launch_bounds__(256)
       for (int h = 0; h < kHeads; ++h)
         if (h0 + h < H) {
 #pragma unroll
-          for (int j = 0; j < N / 2; ++j) turn(a[h].v[2 * j], a[h].v[2 * j + 1], cs[j], sign);
+          for (int j = 0; j < N / 2; ++j)
+            if (rotate && d / 2 + j < half) turn(a[h].v[2 * j], a[h].v[2 * j + 1], cs[j], sign);
           a[h].store(yp + h * ys.head + d);
         }
     }

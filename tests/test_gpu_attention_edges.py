@@ -177,3 +177,32 @@ def test_largest_window_is_no_window(w4, n, kv, dtype):
         got = w4.w4a16_attention(*args, max_q=n, scale=0.1, window=window, lse=lse2)
         assert torch.equal(got, want) and torch.equal(lse, lse2)
     assert w4.w4a16_device_error() == 0
+
+
+# ---- rotation: elements that are copied
+
+def bits_of(x):
+    return x.contiguous().view(torch.int32 if x.dtype == torch.float32 else torch.int16)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("interleaved", [False, True])
+@pytest.mark.parametrize("D,rot", [(128, 64), (128, 20), (64, 18), (72, 40), (64, 64), (128, 2)])
+def test_rope_copies_are_copies(w4, D, rot, interleaved, dtype):
+    """Dims from rot on, and whole tokens whose position is outside the table, come through bit for bit: infinities
+    and signed zeros beside other values too."""
+    T, H, P = 9, 5, 50
+    x = torch.randn(T, H, D, generator=gen(D + rot), device="cuda").to(DT[dtype])
+    odd = torch.tensor([math.inf, 1.0, -math.inf, 0.0, -0.0, -2.0, 3.0, -0.0], device="cuda").to(DT[dtype])
+    x[..., rot:] = odd.repeat(D // 8 + 1)[:D - rot]
+    pos = torch.randint(0, P, (T,), generator=gen(2), device="cuda", dtype=torch.int32)
+    bad = torch.tensor([2, 5], device="cuda")
+    pos[2], pos[5] = -1, P
+    x[bad] = odd.repeat(D // 8)
+    tab = w4.w4a16_rope_table(P, rot)
+    for inverse in (False, True):
+        y = w4.w4a16_rope(x, pos, tab, interleaved=interleaved, inverse=inverse)
+        assert w4.w4a16_device_error() == 1
+        assert torch.equal(bits_of(y[bad]), bits_of(x[bad]))
+        assert torch.equal(bits_of(y[..., rot:]), bits_of(x[..., rot:]))
+        assert torch.isfinite(y[0, :, :rot]).all()
