@@ -190,7 +190,6 @@ __global__ void __launch_bounds__(kWarps * 32, NG <= 4 && NB == 1 && sizeof(T) =
           }
       float f = a.scale * 1.44269504088896340736f * exp2i(e - 14);  // to log2 units
       if constexpr (!kTwo) {
-        f *= kRawUnit;
 #pragma unroll
         for (int i2 = 0; i2 < NG; ++i2) {  // -8 * sum of the group's queries, in the raw codes' units
           float v = 0.0f;
@@ -295,6 +294,12 @@ __global__ void __launch_bounds__(kWarps * 32, NG <= 4 && NB == 1 && sizeof(T) =
             sc[blk][nb][3] = fmaf(d[3], s1, sc[blk][nb][3]);
           }
         }
+      }
+      if (!kTwo) {  // (the factor times the raw codes' unit would pass float32's range for queries of 2^121)
+#pragma unroll
+        for (int nb = 0; nb < NB; ++nb)
+#pragma unroll
+          for (int k = 0; k < 4; ++k) sc[0][nb][k] *= kRawUnit, sc[1][nb][k] *= kRawUnit;
       }
       float mx[NB][2];
 #pragma unroll

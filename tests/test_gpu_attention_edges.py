@@ -206,3 +206,37 @@ def test_rope_copies_are_copies(w4, D, rot, interleaved, dtype):
         assert torch.equal(bits_of(y[bad]), bits_of(x[bad]))
         assert torch.equal(bits_of(y[..., rot:]), bits_of(x[..., rot:]))
         assert torch.isfinite(y[0, :, :rot]).all()
+
+
+# ---- queries near the largest number
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [1])
+@pytest.mark.parametrize("e", [100, 119, 122, 124, 126])
+def test_huge_queries(w4, n, e, dtype):
+    """Queries of 2^e with scores inside float32's range: one key takes all the weight; over zero keys all weigh the
+    same."""
+    G, D, page, kv = 8, 128, 16, 20 + n
+    cache, bt, keys, values = build_cache([kv], 1, D, page, 6)
+    q = torch.zeros(n, G, D, device="cuda")
+    q[..., 5] = 2.0 ** e
+    q = q.to(DT[dtype])
+    lse = torch.empty(n, G, device="cuda")
+    args = (i32(kv), i32(0, n))
+    got = w4.w4a16_attention(q, cache, bt, *args, max_q=n, scale=0.01, lse=lse, causal=False)
+    top = keys[0][:, 0, 5].topk(2).values
+    assert (top[0] - top[1]) * 0.01 * 2.0 ** e > 2.0 ** 20           # (the others weigh nothing)
+    best = keys[0][:, 0, 5].argmax()
+    # weights are exact (one key), the output is rounded to the type; exp2, sums and the quotient: a few 2^-23
+    want = values[0][best, 0].expand(n, G, D)
+    assert ((got.double() - want).abs() <= want.abs() * (STEP[dtype] * (1 + 2.0 ** -6) + 2.0 ** -20)).all()
+    score = top[0] * float(np.float32(0.01)) * 2.0 ** e
+    assert ((lse.double() - score).abs() <= score * 2.0 ** -20).all()
+    k = torch.zeros(kv, 1, D, device="cuda")
+    zero = torch.full_like(cache, 255)
+    slots = bt[0].long()[torch.arange(kv, device="cuda") // page] * page + torch.arange(kv, device="cuda") % page
+    w4.w4a16_kv_append(zero, k, torch.randn(kv, 1, D, generator=gen(3), device="cuda"), slots)
+    got = w4.w4a16_attention(q, zero, bt, *args, max_q=n, scale=0.01, lse=lse, causal=False)
+    v = w4.w4a16_kv_read(zero, slots, D)[1].double()
+    check(q, got, lse, reference(q, [k.double()], [v], [n], [kv], 0.01, False, 0, None), dtype)
+    assert w4.w4a16_device_error() == 0
