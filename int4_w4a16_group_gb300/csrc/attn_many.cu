@@ -56,6 +56,11 @@ static_assert(kSoftWarps * kRegsSoft + kDeqWarps * kRegsDeq + 4 * kRegsRest <= k
 constexpr int kRawStages = 3, kOps = 3, kInfos = 8;
 constexpr float kLag = 8.0f;     // binades a row's maximum may grow before O is rescaled
 constexpr float kTop = 7.0f;     // P's largest value when it has not grown: 2^7
+// Products are below 2^37, so with factors up to this scores stay below 2^20, and the weights multiply and subtract
+// in one rounding. With larger ones the unrounded product and the rounded maximum could differ by more binades than a
+// weight has room for, so the scores are rounded first, in a pass of their own. (Two roundings for all cost 841 .. 859
+// us where one takes 795, the test for this pass 802: 4096 tokens over 8192 keys.)
+constexpr float kFusedFactor = 0x1p-17f;
 
 template <int NG>
 struct Smem {
@@ -266,6 +271,19 @@ __device__ __forceinline__ void scale_weights(uint32_t taddr, uint32_t f2) {
   asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};\n" ::"r"(taddr), "r"(r[0]),
                "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
                : "memory");
+}
+
+// Multiplies a row's scores by f where they lie. Out of line: it hardly ever runs (inlined, every tile pays: 817 us).
+__device__ __noinline__ void scale_scores(uint32_t taddr, float f) {
+#pragma unroll 1
+  for (int q = 0; q < kKeys / 16; ++q) {
+    uint32_t x[16];
+    tmem_ld16(taddr + 16 * q, x);
+#pragma unroll
+    for (int k = 0; k < 16; ++k) x[k] = __float_as_uint(__fmul_rn(__uint_as_float(x[k]), f));
+    tmem_st16(taddr + 16 * q, x);
+  }
+  tmem_wait_st();
 }
 
 template <int NG>
@@ -789,7 +807,7 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           // never 0, which would turn hidden keys' -inf into NaN: zero queries over small keys reach 2^-215
           // (scores are below 2^37 in these units, so a larger ft leaves them at 0 all the same)
-          const float ft = fmaxf(f_row * exp2i(ti.k_exp - kNorm), 0x1p-126f);
+          float ft = fmaxf(f_row * exp2i(ti.k_exp - kNorm), 0x1p-126f);
           if (!full) {  // hidden keys' scores become -inf, in TMEM
 #pragma unroll 1
             for (int q = 0; q < kKeys / 16; ++q) {
@@ -802,6 +820,10 @@ __global__ void __launch_bounds__(kThreads, 1)
               tmem_st16(S + 16 * q, x);
             }
             tmem_wait_st();
+          }
+          if (__any_sync(0xFFFFFFFFu, ft > kFusedFactor)) {  // such a row's scores become what they are, in TMEM
+            scale_scores(S, ft > kFusedFactor ? ft : 1.0f);
+            ft = ft > kFusedFactor ? 1.0f : ft;  // (a row's result does not depend on its neighbours)
           }
           // Weights under the maximum so far, 32 keys at a time, over S's columns (always behind what has
           // been read). Where a row's maximum is too low (8 binades; on an item's first keys) it is

@@ -211,7 +211,7 @@ def test_rope_copies_are_copies(w4, D, rot, interleaved, dtype):
 # ---- queries near the largest number
 
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
-@pytest.mark.parametrize("n", [1])
+@pytest.mark.parametrize("n", [1, 40])
 @pytest.mark.parametrize("e", [100, 119, 122, 124, 126])
 def test_huge_queries(w4, n, e, dtype):
     """Queries of 2^e with scores inside float32's range: one key takes all the weight; over zero keys all weigh the
