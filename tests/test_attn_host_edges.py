@@ -112,3 +112,12 @@ X, P, Y = 0x10000, 0x20000, 0x30000   # fake, aligned: the check must fail befor
 def test_rope_refuses_outputs_that_overlap(lib, T, token, H, head, D):
     for dtype in (0, 1):
         assert lib.w4a16_rope(X, H * D, D, dtype, T, H, D, P, P, 16, 8, 0, 0, Y, token, head, None) == 1
+
+
+def test_cache_calls_of_too_many_tokens(lib):
+    """Token counters are 32 bits wide and step past the end: 2^31 - 1 tokens (keys and values by a stride of zero)
+    would wrap. Both pointers are misaligned, which is refused next: no call gets as far as a launch."""
+    limit = 2 ** 31 - 1 - 2 ** 24
+    for T, status in ((limit, 2), (limit + 1, 3), (2 ** 31 - 1, 3)):
+        assert lib.w4a16_kv_append(X + 4, 0, 128, X + 4, 0, 128, 0, T, 8, 128, P, None, None, 0, 0, 0, Y, 4, 64, None) == status
+        assert lib.w4a16_kv_read(Y, 4, 64, 8, 128, P, T, X + 4, X + 4, None) == status
