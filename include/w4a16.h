@@ -292,7 +292,8 @@ size_t w4a16_kv_page_bytes(int Hkv, int D, int page_size);
  * the nearest float32, which decides their codes. A token whose slot is past the cache or whose
  * position is outside the table is skipped and flagged; a group with a value that is not finite or
  * not below 2^64 in magnitude is stored as zeros and flagged, so a cache written here holds finite
- * values only. */
+ * values only. T at most 2^31 - 2^24 - 1 and Hkv * D at most 2^26 - 2^10, else W4A16_ERR_UNSUPPORTED (reading back
+ * too). */
 w4a16_status w4a16_kv_append(const void* k, int64_t k_token, int64_t k_head, const void* v,
                              int64_t v_token, int64_t v_head, int dtype, int T, int Hkv, int D,
                              const int64_t* slots, const int32_t* positions, const float* table,

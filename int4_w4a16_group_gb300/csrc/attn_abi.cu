@@ -32,6 +32,10 @@ inline bool strides_ok(int dtype, int64_t token, int64_t head) {
 
 // The cache's kernels step through tokens with 32-bit counters, up to a whole grid (below 2^24) past the last one.
 constexpr int kMaxCacheTokens = INT_MAX - (1 << 24);
+// They have a thread for every 8 dims of a token's keys and values, in at most 65535 rows of blocks of 256.
+inline bool cache_grid_ok(int T, int Hkv, int D) {
+  return T <= kMaxCacheTokens && (long long)Hkv * (D / 4) <= 65535ll * 256;
+}
 
 inline w4a16_status check_cache(const void* cache, int num_pages, int page_size, int Hkv, int D) {
   if (Hkv <= 0 || num_pages < 0 || D <= 0) return W4A16_ERR_ARG;
@@ -96,7 +100,7 @@ w4a16_status w4a16_kv_append(const void* k, int64_t k_token, int64_t k_head, con
   if (st != W4A16_OK) return st;
   if (!dtype_ok(dtype) || T < 0 || rot < 0 || rot % 2 != 0 || rot > D) return W4A16_ERR_ARG;
   if (rot > 0 && P <= 0) return W4A16_ERR_ARG;
-  if (T > kMaxCacheTokens) return W4A16_ERR_UNSUPPORTED;
+  if (!cache_grid_ok(T, Hkv, D)) return W4A16_ERR_UNSUPPORTED;
   if (T == 0) return W4A16_OK;
   if (!k || !v || !slots || (rot > 0 && (!positions || !table))) return W4A16_ERR_ARG;
   if (!aligned16(k) || !aligned16(v) || ((uintptr_t)slots & 7u)) return W4A16_ERR_ALIGN;
@@ -115,7 +119,7 @@ w4a16_status w4a16_kv_read(const void* cache, int num_pages, int page_size, int 
   const w4a16_status st = check_cache(cache, num_pages, page_size, Hkv, D);
   if (st != W4A16_OK) return st;
   if (T < 0) return W4A16_ERR_ARG;
-  if (T > kMaxCacheTokens) return W4A16_ERR_UNSUPPORTED;
+  if (!cache_grid_ok(T, Hkv, D)) return W4A16_ERR_UNSUPPORTED;
   if (T == 0) return W4A16_OK;
   if (!slots || !k || !v) return W4A16_ERR_ARG;
   if (!aligned16(k) || !aligned16(v) || ((uintptr_t)slots & 7u)) return W4A16_ERR_ALIGN;

@@ -121,3 +121,13 @@ def test_cache_calls_of_too_many_tokens(lib):
     for T, status in ((limit, 2), (limit + 1, 3), (2 ** 31 - 1, 3)):
         assert lib.w4a16_kv_append(X + 4, 0, 128, X + 4, 0, 128, 0, T, 8, 128, P, None, None, 0, 0, 0, Y, 4, 64, None) == status
         assert lib.w4a16_kv_read(Y, 4, 64, 8, 128, P, T, X + 4, X + 4, None) == status
+
+
+def test_cache_calls_of_too_many_heads(lib):
+    """A token's threads are counted in 32 bits: 2^27 heads of 64 dims came to zero, and a division by it ended the
+    process. As above, calls that are taken are refused for their pointers."""
+    for D in (64, 128, 256):
+        limit = 65535 * 256 // (D // 4)
+        for Hkv, status in ((limit, 2), (limit + 1, 3), (2 ** 33 // D, 3), (2 ** 31 - 1, 3)):
+            assert lib.w4a16_kv_append(X + 4, 0, 128, X + 4, 0, 128, 0, 1, Hkv, D, P, None, None, 0, 0, 0, Y, 4, 64, None) == status
+            assert lib.w4a16_kv_read(Y, 4, 64, Hkv, D, P, 1, X + 4, X + 4, None) == status
