@@ -6,9 +6,10 @@
 namespace w4a16 {
 namespace {
 
-// bf16 sequences of more rows per key/value head than this go to the tcgen05 kernel. 4 sequences of 6000
-// tokens, 8 rows a token (few / many, us): 24 rows 33 / 42, 32 rows 33 / 42, 48 rows 42 / 42, 64 rows
-// 51 / 43, 128 rows 89 / 45, 256 rows 158 / 55. float32 calls and heads of 256 dims have no such kernel:
+// bf16 sequences of more rows per key/value head than this go to the tcgen05 kernel. 8 rows a token, heads of 128
+// (few / many, us): 4 sequences of 6000 tokens: 24 rows 34 / 41, 32 rows 34 / 41, 48 rows 43 / 43, 64 rows 52 / 43,
+// 128 rows 91 / 45, 256 rows 163 / 55; 32 of 2000: 24 rows 71 / 81, 32 rows 74 / 84, 48 rows 100 / 85, 64 rows 129 /
+// 85; one of 6000: 32 rows 22 / 25, 64 rows 25 / 26, 128 rows 35 / 28. float32 calls and heads of 256 dims have no such kernel:
 // their rows go through the other in tiles of 16 (8), which read the keys from L2 again.
 constexpr int kManyRows = 32;
 

@@ -190,8 +190,8 @@ constexpr int kItemCost = 12, kManyItemCost = 4;
 
 // The line: sequences in order; within one, heads; within a head, row tiles; within a row tile, the
 // tiles of keys that any of its rows sees (one empty tile where there are none, so that its rows are
-// written), after kItemCost places that stand for the item's fixed cost. Sequences whose rows are not in (min_rows, max_rows] belong to another kernel. All
-// threads of a CTA walk together: total() and seek() contain barriers.
+// written), after kItemCost places that stand for the item's fixed cost. Sequences whose rows are not in
+// (min_rows, max_rows] belong to another kernel. All threads of a CTA walk together: total() and seek() contain barriers.
 template <int tile_keys, int R, int cost>
 struct Walk {
   const AttnArgs& a;

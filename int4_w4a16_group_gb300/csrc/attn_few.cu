@@ -29,12 +29,14 @@
 // turn, each with its own ring of bulk copies (a tile is one contiguous piece of a page) and its own
 // running softmax, merged through shared memory at the end of an item: no barrier in the loop.
 //
-// What bounds it: instruction issue. A tile of 32 keys (D = 128, 8 rows) takes some 500 instructions for
-// unpacking, products, scaling and the softmax, issued at 2.3 per SM cycle; DRAM reads are the cache's
-// bytes once (205.6 MB for 205.5). One token of 64 sequences of 100 .. 16384 tokens, 64 query and 8
-// key/value heads, bf16: 62 us, 3.3 TB/s; one of 131071 tokens, float32 (twice the products, three terms
-// of P'): 61 us, 2.5 TB/s; one of 333: 13 us, two launches' latency; 16 draft tokens of 4 sequences, float32,
-// 8 row tiles over the same keys: 172 us. Three CTAs per SM (168 registers)
+// What bounds it: latency, with few warps to hide it. A tile of 32 keys (D = 128, 8 rows) is a chain of some 500
+// instructions a warp (load, unpack, product, scale, maximum, exponential, product), and the registers leave 2.8 warps
+// per scheduler (float32, 16 rows: 2): 55 % (48 %) of the issue slots are used, and the most frequent reason for a warp
+// to wait is the fixed latency of the instruction before. DRAM reads are the cache's bytes once (205.6 MB for
+// 205.5). One token of 64 sequences of 100 .. 16384 tokens, 64 query and 8 key/value heads, bf16: 64 us, 3.2 TB/s; one
+// of 131071 tokens, float32 (twice the products, three terms of P'): 62 us, 2.4 TB/s; one of 333: 14 us, of which two
+// launches are 5: its warps wait at the barriers of the walk and the merge and for instructions that run for the first
+// time; 16 draft tokens of 4 sequences, float32, 8 row tiles over the same keys: 174 us. Three CTAs per SM (168 registers)
 // beat four (128, spilling) by 5 to 10 us for the bf16 form with 8 rows.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -123,7 +125,8 @@ __global__ void __launch_bounds__(kWarps * 32, NG <= 4 && NB == 1 && sizeof(T) =
     // page of lane's block (lane 0, 1) of a tile, or -1
     auto page_id = [&](int tile) {
       const int key = key0 + tile * kTile + (lane & 1) * kKvBlock;
-      return (lane < 2 && tile < t_end && key + kKvBlock > key_lo && key < key_end) ? __ldg(bt + (key >> page_shift)) : -1;
+      return (lane < 2 && tile < t_end && key + kKvBlock > key_lo && key < key_end) ? __ldg(bt + (key >> page_shift))
+                                                                                    : -1;
     };
     uint32_t valid = 0;  // two bits per stage: the tile's blocks that were copied
     auto issue = [&](int tile, int stage, int page) {

@@ -9,8 +9,9 @@
 // a power of two per tile of keys (K) and per item (V, kept until a larger scale comes) holds them
 // below 2^15 whatever the scales are. Queries are exact in fp16 after a power of two per row. P is
 // fp16 below 2^15: the maximum that is subtracted lags by up to 8 binades (2^7 .. 2^15 at the top), so
-// O (and the tile's earlier P, rounded once more then) is rescaled only when a row's maximum has grown
-// by more than that. Sums are float32.
+// O (and the tile's earlier P, by a factor rounded to fp16 and rounded once more, 2 x 2^-11, where the output's
+// own rounding is 2^-8; the sum takes the exact factor) is rescaled only when a row's maximum has grown
+// by more than that. Weights under 2^-31 of a row's largest lose bits. Sums are float32.
 //
 // Roles (640 threads, one CTA per SM, persistent over an equal run of the line of key tiles):
 //   warps 0-7   softmax, four per row tile (TMEM lane = row); queries in, outputs out;
@@ -21,12 +22,13 @@
 //   warp 17     issues the MMAs: per key tile and row tile P V' of this tile, then S of the next, which
 //               overwrites the P just used (MMAs of one thread run in order).
 //
-// What bounds it: the hand-offs and the instruction cache. 4096 tokens over 8192 keys, 64 query and 8
-// key/value heads of 128: 829 us, 995 TFLOP/s, 0.52 of the measured bf16 rate. A key tile takes some 4400
-// cycles where its MMAs take 2050: a row tile's softmax (2600) and its MMAs with their two hand-offs (1700)
-// follow one another, and only the other row tile's overlap them. Code that runs once per item costs some
-// 12 cycles an instruction (the roles' code together exceeds the instruction cache), so it is kept in loops;
-// a change of items takes 11000 cycles, of which the queries' loads are 4600.
+// What bounds it: the chain of hand-offs. 4096 tokens over 8192 keys, 64 query and 8 key/value heads of 128: 799 us,
+// 1032 TFLOP/s, 0.54 of the measured bf16 rate; the tensor pipe is busy for 45 % of the cycles. A key tile takes some
+// 4200 cycles where its MMAs take 2050: a row tile's softmax (2600) and its MMAs with their two hand-offs (1700)
+// follow one another, and only the other row tile's overlap them. 59 % of the issue slots are used; of the 8.5 cycles
+// that a warp takes per instruction, 2.8 go to loads of long latency, 1.2 to the latency of the instruction before, 0.9
+// to barriers, 0.35 to fetching instructions. A change of items takes 11000 cycles,
+// of which the queries' loads are 4600.
 // The dims of K' and Q are stored in the order the nibbles unpack in (0 4 1 5 2 6 3 7), and the keys of
 // V' and P rotated within each 8 by the chunk's index, so that neither side reorders anything and the
 // reads of V's rows fall on different banks.
@@ -69,7 +71,7 @@ struct Smem {
   static constexpr int q_tile = kRows * D * 2;
   static constexpr int ops = 2 * q_tile;                        // 3 x K' or V'
   static constexpr int op_tile = kKeys * D * 2;
-  static constexpr int raw = ops + kOps * op_tile;              // 2 x 8 blocks
+  static constexpr int raw = ops + kOps * op_tile;              // 3 x 8 blocks
   static constexpr int block = kKvBlock * (D + D / 8);
   static constexpr int raw_tile = kKeys / kKvBlock * block;
   static constexpr int bars = raw + kRawStages * raw_tile;
@@ -173,8 +175,7 @@ __device__ __forceinline__ uint32_t draft_bits(const AttnArgs& a, int token, int
 }
 
 // The part of a wait that does not succeed at once: polls until the phase completes, another role gave
-// up, or kPolls polls (a second or more) have passed. Kept short: it is inlined at every wait, and the
-// roles' code together is larger than the instruction cache.
+// up, or kPolls polls (a second or more) have passed. Kept short: it is inlined at every wait.
 constexpr int kPolls = 1 << 24;
 __device__ __forceinline__ bool wait_slow(uint32_t bar, uint32_t parity, uint32_t abort_at, unsigned int* err) {
 #pragma unroll 1
@@ -491,89 +492,89 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!wait_warp(kRawFull + s, ph) || !wait_warp(kRawSeen + s, ph)) break;
       const TileInfo ti = info[n % kInfos];
       const uint32_t st = sb + L::raw + s * L::raw_tile;
-        // K': a thread takes word w of every group of a key
-        // K's slot held V of tile n - 2, V's slot K of tile n - 1. Even and odd tiles have barriers of
-        // their own: the one waited on cannot move on another phase before this tile is handed over.
-        if (n >= 2 && !wait_warp(kVFreed + (n & 1), ((n >> 1) & 1) ^ 1)) break;
-        uint32_t op = sb + L::ops + slot * L::op_tile;
-        {
-          const float f = exp2i(kNorm - ti.k_exp);
-          const int word = lane >> 3;
+      // K': a thread takes word w of every group of a key
+      // K's slot held V of tile n - 2, V's slot K of tile n - 1. Even and odd tiles have barriers of
+      // their own: the one waited on cannot move on another phase before this tile is handed over.
+      if (n >= 2 && !wait_warp(kVFreed + (n & 1), ((n >> 1) & 1) ^ 1)) break;
+      uint32_t op = sb + L::ops + slot * L::op_tile;
+      {
+        const float f = exp2i(kNorm - ti.k_exp);
+        const int word = lane >> 3;
 #pragma unroll 1
-          for (int p = 0; p < kKeys / (8 * kDeqWarps); ++p) {
-            const int key = (p * kDeqWarps + dw) * 8 + (lane & 7);
+        for (int p = 0; p < kKeys / (8 * kDeqWarps); ++p) {
+          const int key = (p * kDeqWarps + dw) * 8 + (lane & 7);
+          const uint32_t blk = st + (key / kKvBlock) * L::block;
+          const int r = key % kKvBlock;
+          uint32_t cw[NG], sw[NG / 2];
+          lds_words<NG>(blk + r * (D / 2) + ((word ^ (r & 2)) * NG) * 4, cw);
+          lds_words<NG / 2>(blk + kv_scales_off(D, 0) + r * NG * 2, sw);
+          const uint32_t row = op + (uint32_t)(key >> 3) * 1024u + (uint32_t)(key & 7) * 128u;
+#pragma unroll
+          for (int i = 0; i < NG; ++i) {
+            const float sc = bf16_of(sw, i) * f;
+            const uint32_t s2 = pack_half2(sc, sc);
+            uint32_t x[4];
+            unpack_word(cw[i], x);
+            const int chunk = 4 * i + word;
+            sts128(row + (chunk >> 3) * (kKeys * 128) + (((chunk & 7) ^ (key & 7)) << 4),
+                   hmul2_u32(x[0], s2), hmul2_u32(x[1], s2), hmul2_u32(x[2], s2), hmul2_u32(x[3], s2));
+          }
+        }
+      }
+      tc::fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) tc::mbar_arrive(bar(kOpFull + slot));
+      if (++slot == kOps) slot = 0;
+      // V'^T: a thread takes one word of 8 keys (rotated by its chunk) and writes 8 dim rows
+      if (n >= 1 && !wait_warp(kKFreed + ((n - 1) & 1), ((n - 1) >> 1) & 1)) break;
+      op = sb + L::ops + slot * L::op_tile;
+      {
+        const float f = exp2i(kNorm - ti.v_exp);
+        const int word = dw & 3, ch = dw >> 2, cc = lane & 7, i = lane >> 3;
+        if (i < NG) {
+          uint32_t cw[8];
+          float sc[8];
+#pragma unroll
+          for (int k = 0; k < 8; ++k) {
+            const int key = ch * 64 + cc * 8 + ((k + cc) & 7);
             const uint32_t blk = st + (key / kKvBlock) * L::block;
             const int r = key % kKvBlock;
-            uint32_t cw[NG], sw[NG / 2];
-            lds_words<NG>(blk + r * (D / 2) + ((word ^ (r & 2)) * NG) * 4, cw);
-            lds_words<NG / 2>(blk + kv_scales_off(D, 0) + r * NG * 2, sw);
-            const uint32_t row = op + (uint32_t)(key >> 3) * 1024u + (uint32_t)(key & 7) * 128u;
-#pragma unroll
-            for (int i = 0; i < NG; ++i) {
-              const float sc = bf16_of(sw, i) * f;
-              const uint32_t s2 = pack_half2(sc, sc);
-              uint32_t x[4];
-              unpack_word(cw[i], x);
-              const int chunk = 4 * i + word;
-              sts128(row + (chunk >> 3) * (kKeys * 128) + (((chunk & 7) ^ (key & 7)) << 4),
-                     hmul2_u32(x[0], s2), hmul2_u32(x[1], s2), hmul2_u32(x[2], s2), hmul2_u32(x[3], s2));
-            }
+            asm volatile("ld.shared.u32 %0, [%1];\n"
+                         : "=r"(cw[k])
+                         : "r"(blk + kv_codes_off(D, 1) + r * (D / 2) + ((word ^ (r & 2)) * NG + i) * 4));
+            const uint32_t b = lds_u16(blk + kv_scales_off(D, 1) + (r * NG + i) * 2);
+            sc[k] = __uint_as_float(b << 16) * f;
           }
-        }
-        tc::fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) tc::mbar_arrive(bar(kOpFull + slot));
-        if (++slot == kOps) slot = 0;
-        // V'^T: a thread takes one word of 8 keys (rotated by its chunk) and writes 8 dim rows
-        if (n >= 1 && !wait_warp(kKFreed + ((n - 1) & 1), ((n - 1) >> 1) & 1)) break;
-        op = sb + L::ops + slot * L::op_tile;
-        {
-          const float f = exp2i(kNorm - ti.v_exp);
-          const int word = dw & 3, ch = dw >> 2, cc = lane & 7, i = lane >> 3;
-          if (i < NG) {
-            uint32_t cw[8];
-            float sc[8];
+          uint32_t s2[4];
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const int key = ch * 64 + cc * 8 + ((k + cc) & 7);
-              const uint32_t blk = st + (key / kKvBlock) * L::block;
-              const int r = key % kKvBlock;
-              asm volatile("ld.shared.u32 %0, [%1];\n"
-                           : "=r"(cw[k])
-                           : "r"(blk + kv_codes_off(D, 1) + r * (D / 2) + ((word ^ (r & 2)) * NG + i) * 4));
-              const uint32_t b = lds_u16(blk + kv_scales_off(D, 1) + (r * NG + i) * 2);
-              sc[k] = __uint_as_float(b << 16) * f;
-            }
-            uint32_t s2[4];
-#pragma unroll
-            for (int q = 0; q < 4; ++q) s2[q] = pack_half2(sc[2 * q], sc[2 * q + 1]);
-            const uint32_t row = op + ch * (D * 128) + (uint32_t)(4 * i + word) * 1024u;
+          for (int q = 0; q < 4; ++q) s2[q] = pack_half2(sc[2 * q], sc[2 * q + 1]);
+          const uint32_t row = op + ch * (D * 128) + (uint32_t)(4 * i + word) * 1024u;
 #pragma unroll 1
-            for (int hf = 0; hf < 2; ++hf) {  // dims 0 .. 3, then 4 .. 7 of the word
-              const uint32_t sel = hf ? 0x7632u : 0x5410u;
-              uint32_t o[4][4];
+          for (int hf = 0; hf < 2; ++hf) {  // dims 0 .. 3, then 4 .. 7 of the word
+            const uint32_t sel = hf ? 0x7632u : 0x5410u;
+            uint32_t o[4][4];
 #pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                uint32_t x[4];
-                unpack_word(prmt(cw[2 * q], cw[2 * q + 1], sel), x);
+            for (int q = 0; q < 4; ++q) {
+              uint32_t x[4];
+              unpack_word(prmt(cw[2 * q], cw[2 * q + 1], sel), x);
 #pragma unroll
-                for (int j = 0; j < 4; ++j) o[j][q] = hmul2_u32(x[j], s2[q]);
-              }
-#pragma unroll
-              for (int j = 0; j < 4; ++j)
-                sts128(row + (4 * hf + j) * 128u + ((cc ^ (4 * hf + j)) << 4), o[j][0], o[j][1], o[j][2], o[j][3]);
+              for (int j = 0; j < 4; ++j) o[j][q] = hmul2_u32(x[j], s2[q]);
             }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              sts128(row + (4 * hf + j) * 128u + ((cc ^ (4 * hf + j)) << 4), o[j][0], o[j][1], o[j][2], o[j][3]);
           }
         }
-        tc::fence_proxy_async();
-        __syncwarp();
-        if (lane == 0) {
-          tc::mbar_arrive(bar(kOpFull + slot));
-          tc::mbar_arrive(bar(kRawEmpty + s));
-        }
-        if (++slot == kOps) slot = 0;
-        if (++s == kRawStages) s = 0, ph ^= 1u;
-        if (ti.flags & kEnd) break;
+      }
+      tc::fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) {
+        tc::mbar_arrive(bar(kOpFull + slot));
+        tc::mbar_arrive(bar(kRawEmpty + s));
+      }
+      if (++slot == kOps) slot = 0;
+      if (++s == kRawStages) s = 0, ph ^= 1u;
+      if (ti.flags & kEnd) break;
     }
   } else if (warp == kMmaWarp) {
     // ---- MMAs. The whole warp walks along and one elected lane issues: descriptors then stay in uniform

@@ -12,9 +12,9 @@
 // piece (D = 128), and nothing is staged. A thread keeps its (K or V, head, word) and walks over
 // tokens, so that the index arithmetic is done once; quotients are reciprocal products, corrected
 // where they are close to a border. 16384 tokens of 8 heads of 128 (bf16, rotated), append and read back: 107 us with
-// 64-bit index divisions per word and IEEE quotients, 88 us now (54 + 34). Appending is bound by
+// 64-bit index divisions per word and IEEE quotients, 85 us now (52 + 34). Appending is bound by
 // instruction issue (350 a warp and 32 words, most of them the rotation, the exact rounding and the packing,
-// at 2.9 per SM cycle), reading back by its float32 stores (134 MB, 4.6 TB/s with the loads).
+// at 2.9 per SM cycle, 72 % of the slots) and its loads' latency, reading back by its float32 stores (134 MB, 4.6 TB/s with the loads).
 #include <cuda_bf16.h>
 
 #include "attn.h"
@@ -46,7 +46,8 @@ __device__ __forceinline__ void load8(const __nv_bfloat16* p, float (&v)[8]) {
 __device__ __forceinline__ float load1(const float* p) { return __ldg(p); }
 __device__ __forceinline__ float load1(const __nv_bfloat16* p) { return __bfloat162float(*p); }
 
-// a * c + b * s, rounded once: products exact as (p + e), sum exact as (h + l).
+// a * c + b * s, rounded once: products exact as (p + e), by FMA (Ogita, Rump, Oishi, "Accurate Sum and Dot Product",
+// 2005), sum exact as (h + l) (Knuth, "The Art of Computer Programming", vol. 2, 4.2.2).
 __device__ __forceinline__ float dot2_rn(float a, float c, float b, float s) {
   const float p = __fmul_rn(a, c), pe = __fmaf_rn(a, c, -p);
   const float q = __fmul_rn(b, s), qe = __fmaf_rn(b, s, -q);
