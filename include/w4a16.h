@@ -319,7 +319,8 @@ w4a16_status w4a16_kv_read(const void* cache, int num_pages, int page_size, int 
  *               sequence's n draft tokens, and draft token d if bit d % 32 of word d / 32 of its row
  *               is set (drafts past the row's words are not seen). Not with a window; causal is 1.
  *               A draft that no row sees takes no part, whatever the cache holds at its place.
- * A row that sees no key is zero with lse = -inf. lse [T, Hq] (or NULL) receives
+ * Every key that a query token sees has been appended (its scales are finite); what the cache holds at other
+ * keys takes no part. A row that sees no key is zero with lse = -inf. lse [T, Hq] (or NULL) receives
  * ln sum_j exp(scale * q . K[j]). out is [T, Hq, D] contiguous, of q's type.
  * max_q is an upper bound of the sequences' query tokens, known to the host; rows of a sequence with
  * more are not computed, and flagged. A page outside the cache counts as keys that no row sees, and
